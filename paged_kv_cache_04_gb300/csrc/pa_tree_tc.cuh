@@ -99,8 +99,8 @@ struct TreeTc {
   static constexpr unsigned K_OFF = QB * Q_BYTES, V_OFF = K_OFF + KS * TILE, BAR_OFF = V_OFF + VS * TILE;
   static constexpr int KINDS = NS == 2 ? 3 : 1;     // whom a tile is for: stream 0, stream 1, both
   static constexpr int BARS = (KINDS + 1) * (KS + QB) + (KINDS + 3) * VS + 8 * NS + 2;
-  static constexpr unsigned BAD_OFF = BAR_OFF + BARS * 8;            // u64 [VS]
-  static constexpr unsigned ML_OFF = BAD_OFF + VS * 8;               // float2 [2][128]
+  static constexpr unsigned BAD_OFF = BAR_OFF + BARS * 8;            // u64 [2][VS]
+  static constexpr unsigned ML_OFF = BAD_OFF + 2 * VS * 8;           // float2 [2][128]
   static constexpr unsigned SCRATCH_OFF = ML_OFF + (NS == 2 ? 2048 : 0);
   static constexpr unsigned MISC_OFF = SCRATCH_OFF + (THREADS / 32 + 3) * 8;
   static constexpr unsigned TOTAL = MISC_OFF + 16;
@@ -428,6 +428,10 @@ __global__ void __launch_bounds__(TreeTc<D, QR>::THREADS, 1)
   uint64_t* o_free = pv_done + 2 * NS;    // O read at an item's end
   uint64_t* ml_full = o_free + 1;         // both streams' (max, sum) in shared memory
   uint64_t* fin = o_free + 2;             // [2][NS] every product done (teardown)
+  // [2][VS] what the check of a slot's tile found, in two copies that its checked tiles take in turn. A warp reads the
+  // word after its weights have gone off, and the slot may be filled and checked again before it has (at head_dim 256
+  // by a warp three tiles on, which waits for no weights of this one's next tile). It can not be filled a second time:
+  // that takes the output products of the tile in between, and so this warp's weights.
   unsigned long long* bad_rows = reinterpret_cast<unsigned long long*>(smem + C::BAD_OFF);
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
@@ -722,13 +726,14 @@ __global__ void __launch_bounds__(TreeTc<D, QR>::THREADS, 1)
           const int span = two ? 8 : 16, rb = (two ? warp : wq) * span;
           const unsigned bad = tree_check_v<DT, D>(smem + C::V_OFF + vslot * C::TILE, rb, span, it.prefix - t0,
                                                    it.ctx - t0);
+          unsigned long long* word = &bad_rows[vpar * VS + vslot];
           if (NS == 1 || !two) {
             if (lane < NS) {
-              reinterpret_cast<uint16_t*>(&bad_rows[vslot])[wq] = (uint16_t)bad;
+              reinterpret_cast<uint16_t*>(word)[wq] = (uint16_t)bad;
               mbar_arrive(&v_clean[vslot]);
             }
           } else if (lane == 0) {
-            reinterpret_cast<uint8_t*>(&bad_rows[vslot])[warp] = (uint8_t)bad;
+            reinterpret_cast<uint8_t*>(word)[warp] = (uint8_t)bad;
             mbar_arrive(&v_clean[vslot]);
           }
         }
@@ -862,7 +867,7 @@ __global__ void __launch_bounds__(TreeTc<D, QR>::THREADS, 1)
             stop = true;
             break;
           }
-          const unsigned long long bad = bad_rows[vslot];
+          const unsigned long long bad = bad_rows[vpar * VS + vslot];
           if (bad) {  // infinities and NaN of drafted tokens, to the rows that attend them
             tc_fence_after();
             tree_add_bad<DT, D>(p, table, it.kv, t0, bad, live ? seen : 0ull, lanes + w * D);

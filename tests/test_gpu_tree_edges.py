@@ -1,0 +1,55 @@
+"""pa_decode_tree where its tiles meet their limits: values that are not finite over several checked tiles."""
+import os
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from oracle import tree as otree  # noqa: E402
+from tree_harness import Batch, check  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def repeated(b, times, device):
+    """The batch's only sequence `times` times over, all reading the same blocks: several whole items for every CTA."""
+    x = b.gpu(device)
+    for n in ("block_tables", "q", "mask"):
+        if getattr(x, n) is not None:
+            setattr(x, n, getattr(x, n).repeat(times, *[1] * (getattr(x, n).dim() - 1)))
+    x.context_lens, x.N = x.context_lens.repeat(times), b.new[0] * times
+    x.query_starts = torch.arange(times + 1, dtype=torch.int32, device=device) * b.new[0]
+    return x
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 256, "bf16"), (8, 1, 256, "f16"), (1, 1, 256, "bf16"), (8, 1, 128, "bf16"),
+                                   (1, 1, 128, "f16"), (8, 8, 64, "bf16"), (1, 1, 64, "f32")])
+@pytest.mark.parametrize("prefix,new", [(63, 256), (40, 150), (0, 130)])
+def test_values_in_three_to_five_checked_tiles(pa, cuda_device, heads, prefix, new):
+    """One element of V infinite in every checked tile, each in a column of its own: those columns of the rows that
+    attend it, and nothing else; alone and with rings that wrap around within a CTA's items."""
+    H, G, d, t = heads
+    b = Batch(50 + new, [prefix], [new], H, G, d, t, kind="any")
+    nodes = sorted({min(new - 1, max(0, tile * 64 + off - prefix)) for tile, off in zip(range(5), (63, 3, 17, 40, 62))})
+    for c, node in enumerate(nodes):
+        row = torch.randn(G, d).to(b.dtype)
+        row[:, 7 * c + 3] = float("-inf") if c % 2 else float("inf")
+        b.set_row(0, prefix + node, v=row)
+    with np.errstate(invalid="ignore"):
+        ref = b.reference()
+    allow = np.where(np.isfinite(b.allow), b.allow, 0.0)
+    seen = np.array([otree.unpack_row(r, new) for r in b.mask.tolist()])
+    for c, node in enumerate(nodes):
+        assert (np.isinf(ref[:, :, 7 * c + 3]) == seen[:, node, None]).all()
+    finite = np.isfinite(ref)
+    for times in (1, 60):
+        x = repeated(b, times, cuda_device)
+        for out_dtype in (b.dtype, torch.float32):
+            out = x.run(pa, out_dtype=out_dtype).cpu()
+            ok, want = np.tile(finite, (times, 1, 1)), np.tile(ref, (times, 1, 1))
+            assert (out.double().numpy()[~ok] == want[~ok]).all(), f"{heads} {new} x {times}"
+            check(torch.where(torch.from_numpy(ok), out, torch.zeros_like(out)), np.where(ok, want, 0.0),
+                  f"{heads} {new} x {times}", allow=np.tile(allow, (times, 1, 1)))
+    assert pa.pa_get_error() == 0
