@@ -371,7 +371,8 @@ pa_status pa_decode_split_fp8(void* out, const void* q, const void* k_cache, con
  * A sequence whose blocks are not left in the list (PA_DEVERR_NO_BLOCKS), whose
  * row is too short (PA_DEVERR_CONTEXT), or whose tokens pass max_tokens
  * (PA_DEVERR_QUERY) gets nothing: no blocks, slots of -1, context_lens_out 0 (and
- * pa_decode_tree gives it rows of zeros); the caller still has its old lengths.
+ * pa_decode_tree gives it rows of zeros); the caller still has its old lengths. One
+ * without new tokens that holds its blocks needs nothing and is served in any case.
  * Negative lengths count as 0 (PA_DEVERR_CONTEXT). A free block id outside the
  * pool is entered as -1 and its tokens get slots of -1 (PA_DEVERR_BLOCK_ID). A
  * parent that is not below its node counts as -1, and the nodes of a sequence with more than 64 * mask_words of them get no

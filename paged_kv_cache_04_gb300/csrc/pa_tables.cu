@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_tables_kernel(const Build
   // reach for it and for all that follow it and need any.)
   for (int s = b; s < e; ++s) {
     if (per > 1) q = build_seq(p, s);
-    const bool fits = t0 + q.fresh <= p.max_tokens;
+    const bool fits = q.fresh == 0 || t0 + q.fresh <= p.max_tokens;
     const bool blocks = q.need == 0 || b0 + q.need <= avail;
     const bool ok = fits && blocks && q.want <= p.max_blocks;
     starts[s] = (int)min(t0, (long long)p.max_tokens);
