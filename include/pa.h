@@ -371,7 +371,8 @@ pa_status pa_decode_split_fp8(void* out, const void* q, const void* k_cache, con
  * A sequence whose blocks are not left in the list (PA_DEVERR_NO_BLOCKS), whose
  * row is too short (PA_DEVERR_CONTEXT), or whose tokens pass max_tokens
  * (PA_DEVERR_QUERY) gets nothing: no blocks, slots of -1, context_lens_out 0 (and
- * pa_decode_tree gives it rows of zeros); the caller still has its old lengths. One
+ * pa_decode_tree gives it rows of zeros, pa_commit_tree a length of 0); the caller
+ * still has its old lengths, and pa_commit_tree_keep carries them on. One
  * without new tokens that holds its blocks needs nothing and is served in any case.
  * Negative lengths count as 0 (PA_DEVERR_CONTEXT). A free block id outside the
  * pool is entered as -1 and its tokens get slots of -1 (PA_DEVERR_BLOCK_ID). A
@@ -456,6 +457,10 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_cache, const vo
  * blocks that hold drafted tokens. An accepted node that the sequence does not
  * have counts as -1 (PA_DEVERR_QUERY); a row in a block outside the pool is
  * skipped (PA_DEVERR_BLOCK_ID). mask_words at most 4.
+ *
+ * A sequence that pa_build_tables did not serve has context_lens[s] = 0, and so a
+ * new length of 0: a loop that goes on from new_context_lens would forget what it
+ * has cached. Such a loop calls pa_commit_tree_keep (below).
  */
 pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches, int num_layers,
                          const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
@@ -463,6 +468,25 @@ pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches, int num_l
                          const int32_t* accepted, int32_t* new_context_lens, int num_seqs, int num_tokens,
                          int num_kv_heads, int head_dim, int block_size, pa_kv_layout layout, int64_t num_blocks,
                          pa_dtype dtype, cudaStream_t stream);
+
+/*
+ * The same for loops whose steps may leave a sequence unserved (no free blocks, no
+ * token places, a short row): where context_lens[s] is 0, new_context_lens[s] =
+ * context_lens_before[s] (a negative one counts as 0), so that the sequence's cached
+ * tokens stay its context and the next step can serve it.
+ *
+ *   context_lens_before  int32 [num_seqs]: the lengths before the step, as given to
+ *                        pa_build_tables; new_context_lens may be this very array
+ *                        (the step's lengths then move on in place), but not overlap
+ *                        it otherwise. Null: as pa_commit_tree.
+ */
+pa_status pa_commit_tree_keep(void* const* k_caches, void* const* v_caches, int num_layers,
+                              const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                              const int32_t* context_lens_before, const int32_t* query_starts,
+                              const int64_t* tree_mask, int mask_words, const int32_t* accepted,
+                              int32_t* new_context_lens, int num_seqs, int num_tokens, int num_kv_heads,
+                              int head_dim, int block_size, pa_kv_layout layout, int64_t num_blocks, pa_dtype dtype,
+                              cudaStream_t stream);
 
 /*
  * Move KV blocks between two pools in one launch: the GPU <-> CPU swap of

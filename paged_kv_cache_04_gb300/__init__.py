@@ -89,6 +89,7 @@ def library():
     lib.pa_decode_tree_workspace_bytes.restype = SZ
     lib.pa_decode_tree.argtypes = [P, P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, I64, F, I, I, I, P, SZ, P]
     lib.pa_commit_tree.argtypes = [P, P, I, P, I, P, P, P, I, P, P, I, I, I, I, I, I, I64, I, P]
+    lib.pa_commit_tree_keep.argtypes = [P, P, I, P, I, P, P, P, P, I, P, P, I, I, I, I, I, I, I64, I, P]
     lib.pa_get_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), P]
     lib.pa_check_wait_limit.argtypes = [ctypes.c_uint64, P]
     lib.pa_status_string.argtypes = [I]
@@ -120,7 +121,7 @@ def library():
     for f in ("pa_reshape_and_cache", "pa_decode", "pa_decode_split", "pa_decode_split_static",
               "pa_copy_blocks", "pa_swap_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
               "pa_decode_split_fp8", "pa_decode_cascade", "pa_build_tables", "pa_decode_tree", "pa_commit_tree",
-              "pa_get_error", "pa_debug_check", "pa_check_wait_limit",
+              "pa_commit_tree_keep", "pa_get_error", "pa_debug_check", "pa_check_wait_limit",
               "pa_version"):
         getattr(lib, f).restype = I
     _lib = lib
@@ -304,7 +305,7 @@ def _marshal():
         except ImportError as e:
             raise PAError("load", PA_ERR_CUDA, f"{e}: build it with __graft_entry__.build()") from e
         at = [ctypes.cast(f, ctypes.c_void_p).value
-              for f in (lib.pa_build_tables, lib.pa_decode_tree, lib.pa_commit_tree)]
+              for f in (lib.pa_build_tables, lib.pa_decode_tree, lib.pa_commit_tree_keep)]
         _pa_torch.connect(PAError, *at)
         _native = _pa_torch
     return _native
@@ -347,16 +348,20 @@ def pa_decode_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_s
 
 
 def pa_commit_tree(k_caches, v_caches, block_tables, context_lens, query_starts, tree_mask, accepted,
-                   new_context_lens, stream=None, layout="HND"):
+                   new_context_lens, stream=None, layout="HND", context_lens_before=None):
     """Keep each sequence's accepted path: the K/V rows of node ``accepted[s]`` and its ancestors move, in every
     layer, to the rows right behind the context, and ``new_context_lens[s]`` becomes the context's new length.
 
     Arrays as given to ``pa_decode_tree``; ``accepted`` int32 [num_seqs], -1 for none. ``new_context_lens`` may
     not overlap ``context_lens``.
+
+    A sequence that ``pa_build_tables`` did not serve comes with a context of 0 and gets a new length of 0, or, with
+    ``context_lens_before`` (the lengths given to ``pa_build_tables``), the length that it had. A loop whose free list
+    can run dry passes it; ``new_context_lens`` may be the same tensor.
     """
     (_native or _marshal()).commit_tree(
         list(k_caches), list(v_caches), block_tables, context_lens, query_starts, tree_mask, accepted,
-        new_context_lens, None if stream is None else stream.cuda_stream, layout)
+        new_context_lens, None if stream is None else stream.cuda_stream, layout, context_lens_before)
 
 
 def pa_copy_blocks(k_caches, v_caches, block_pairs, stream=None):

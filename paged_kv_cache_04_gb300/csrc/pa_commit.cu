@@ -30,6 +30,7 @@ struct CommitParams {
   const int32_t* block_tables;
   int max_blocks;
   const int32_t *context_lens, *query_starts;
+  const int32_t* before;                // null: a sequence without a context gets length 0; may be new_context_lens
   const unsigned long long* tree_mask;  // null: drafts without branches
   int words;
   const int32_t* accepted;
@@ -117,7 +118,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
       }
     }
     if (bad && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(p.err, bad);
-    if (lead) p.new_context_lens[s] = prefix + kept;
+    // A context of 0 is how an unserved sequence comes here: it keeps the length that it had. (Only this thread reads
+    // the old length, so the new one may be written over it.)
+    if (lead) p.new_context_lens[s] = ctx == 0 && p.before != nullptr ? max(p.before[s], 0) : prefix + kept;
     if (lane == 0) moves = listed;
   }
   __syncthreads();
@@ -172,6 +175,19 @@ extern "C" pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches
                                     int32_t* new_context_lens, int num_seqs, int num_tokens, int num_kv_heads,
                                     int head_dim, int block_size, pa_kv_layout layout, int64_t num_blocks,
                                     pa_dtype dtype, cudaStream_t stream) {
+  return pa_commit_tree_keep(k_caches, v_caches, num_layers, block_tables, max_blocks_per_seq, context_lens, nullptr,
+                             query_starts, tree_mask, mask_words, accepted, new_context_lens, num_seqs, num_tokens,
+                             num_kv_heads, head_dim, block_size, layout, num_blocks, dtype, stream);
+}
+
+extern "C" pa_status pa_commit_tree_keep(void* const* k_caches, void* const* v_caches, int num_layers,
+                                         const int32_t* block_tables, int max_blocks_per_seq,
+                                         const int32_t* context_lens, const int32_t* context_lens_before,
+                                         const int32_t* query_starts, const int64_t* tree_mask, int mask_words,
+                                         const int32_t* accepted, int32_t* new_context_lens, int num_seqs,
+                                         int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                         pa_kv_layout layout, int64_t num_blocks, pa_dtype dtype,
+                                         cudaStream_t stream) {
   using namespace pa;
   if (num_layers <= 0 || num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
       num_blocks <= 0 || max_blocks_per_seq <= 0 || !valid_dtype(dtype) ||
@@ -180,7 +196,7 @@ extern "C" pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches
   if (num_seqs == 0) return PA_OK;
   if (!k_caches || !v_caches || !block_tables || !context_lens || !query_starts || !accepted || !new_context_lens)
     return PA_ERR_INVALID_ARG;
-  const void* words4[] = {block_tables, context_lens, query_starts, accepted, new_context_lens};
+  const void* words4[] = {block_tables, context_lens, context_lens_before, query_starts, accepted, new_context_lens};
   for (const void* q : words4)
     if (reinterpret_cast<uintptr_t>(q) & 3u) return PA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) || (tree_mask != nullptr && mask_words <= 0))
@@ -193,6 +209,7 @@ extern "C" pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches
   struct Span { const void* p; uintptr_t n; };
   const Span ins[] = {{context_lens, bytes}, {accepted, bytes}, {query_starts, bytes + 4},
                       {block_tables, bytes * max_blocks_per_seq},
+                      {context_lens_before, context_lens_before && context_lens_before != new_context_lens ? bytes : 0},
                       {tree_mask, tree_mask ? (uintptr_t)num_tokens * mask_words * 8 : 0}};
   for (const Span& q : ins) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(q.p);
@@ -206,6 +223,7 @@ extern "C" pa_status pa_commit_tree(void* const* k_caches, void* const* v_caches
   p.block_tables = block_tables;
   p.max_blocks = max_blocks_per_seq;
   p.context_lens = context_lens;
+  p.before = context_lens_before;
   p.query_starts = query_starts;
   p.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
   p.words = mask_words;

@@ -28,7 +28,7 @@ using at::Tensor;
 PyObject* g_error = nullptr;  // PAError(func, status, detail)
 decltype(&pa_build_tables) g_build_tables = nullptr;
 decltype(&pa_decode_tree) g_decode_tree = nullptr;
-decltype(&pa_commit_tree) g_commit_tree = nullptr;
+decltype(&pa_commit_tree_keep) g_commit_tree = nullptr;
 
 struct Refused {
   int status;
@@ -217,7 +217,7 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 }
 
 PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded("pa_commit_tree", nargs, 10, [&]() -> int {
+  return guarded("pa_commit_tree", nargs, 11, [&]() -> int {
     Device d;
     const Tensor* first = nullptr;
     auto pools = [&](PyObject* o, std::vector<void*>& ptrs) {
@@ -243,18 +243,20 @@ PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                  &out = tensor(a[7]);
     need(bt.dim() == 2, "block_tables must be 2-D");
     const int64_t S = bt.size(0);
-    need(is_1d(ctx, S) && is_1d(acc, S) && is_1d(out, S) && is_1d(starts, S + 1), "table shapes");
+    const Tensor* before = optional_tensor(a[10]);
+    need(is_1d(ctx, S) && is_1d(acc, S) && is_1d(out, S) && is_1d(starts, S + 1) && (!before || is_1d(*before, S)),
+         "table shapes");
     const Tensor* mask = optional_tensor(a[5]);
     int words = 0;
     const int64_t N = mask && mask->dim() > 0 ? mask->size(0) : 0x7fffffff;
     int64_t* mask_p = mask ? mask_of(d, *mask, N, &words) : nullptr;
     return g_commit_tree(k.data(), v.data(), int32((int64_t)k.size()), i32(d, bt), int32(bt.size(1)), i32(d, ctx),
-                         i32(d, starts), mask_p, words, i32(d, acc), i32(d, out), int32(S), int32(N), p.G, p.D, p.B,
-                         p.layout, p.blocks, dtype_of(*first), d.stream(a[8]));
+                         before ? i32(d, *before) : nullptr, i32(d, starts), mask_p, words, i32(d, acc), i32(d, out),
+                         int32(S), int32(N), p.G, p.D, p.B, p.layout, p.blocks, dtype_of(*first), d.stream(a[8]));
   });
 }
 
-// connect(PAError, address of pa_build_tables, of pa_decode_tree, of pa_commit_tree)
+// connect(PAError, address of pa_build_tables, of pa_decode_tree, of pa_commit_tree_keep)
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (nargs != 4) {
     PyErr_SetString(PyExc_TypeError, "connect takes the error class and three addresses");
