@@ -422,7 +422,8 @@ pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t
  * statistics are fp32. Over 16-bit caches the softmax weights go to the tensor
  * cores in two 16-bit parts, as in pa_decode; where a sequence has more than 128
  * rows (n_s x num_heads / num_kv_heads), head_dim is below 256 and out is 16-bit, in
- * one (an error of up to half a step per weight, like the output's own rounding).
+ * one: a weight is off by up to half a step, like the output's own rounding, and is
+ * summed as it was rounded, so that a row's weights still add up to one.
  * fp32 caches use fp32 arithmetic throughout. num_seqs at most 2^24.
  *
  * Long contexts are split over the GPU whatever the batch: the work is cut into

@@ -52,10 +52,16 @@
 // registers to keep a tile's weights in, so its scores are read once: the weights are
 // taken against the reference so far and kept if their sum shows that none of them is
 // above 2^kTreeRescale, else the tile is read again for a new reference (a pass for
-// the maximum first: 291 us against 261 on that batch). Rounding a weight
-// is off by at most half a step of the type, as the output's own rounding is, and
-// the errors of many weights average out: the result's error grows by up to
-// sqrt(2). An fp32 output keeps both parts everywhere.
+// the maximum first: 291 us against 261 on that batch). A rounded weight w (1 + e) is
+// off by at most half a step of the type. Sum and products take the same rounded
+// weights, so they still make an average, and to first order in e the result is off by
+//   sum w e (v - out) / sum w   <=   half a step x sum w |v - out| / sum w:
+// nothing where one token carries its row or the values are alike, and about the
+// output's own rounding (a total of sqrt(2) times that) where they differ at random.
+// With the weights summed before they are rounded, a row carried by one token would be
+// off by up to half a step more; rounding first costs 268 us against 251 on that batch
+// (sustained, at the power limit: 293 against 284). An fp32 output keeps both parts
+// everywhere.
 //
 // Every wait is bounded; on a timeout all roles stop, copies and products in
 // flight are waited for, and the tensor memory is released.
@@ -356,8 +362,9 @@ static __device__ __noinline__ TreeRef tree_new_ref(uint32_t sp, float scale, fl
 }
 
 // The weights 2^(scale x score + neg) of a row's 64 scores at `sp`, in one 16-bit part, written over the scores'
-// first 32 columns (without a wait), their sum added to `l`. With `check`, not if a sum of the warp's rows allows a
-// weight above 2^kTreeRescale (then: false; tree_new_ref moves references by less, so that it does not come again).
+// first 32 columns (without a wait), their sum added to `l`: of the weights as they were rounded, which are the ones
+// that the output products take. With `check`, not if a sum of the warp's rows allows a weight above 2^kTreeRescale
+// (then: false; tree_new_ref moves references by less, so that it does not come again).
 template <typename DT>
 __device__ __forceinline__ bool tree_weights(uint32_t sp, float scale, float neg, bool check, float& l) {
   const uint64_t scale2 = pair2(scale, scale), neg2 = pair2(neg, neg);
@@ -374,8 +381,10 @@ __device__ __forceinline__ bool tree_weights(uint32_t sp, float scale, float neg
       unpair2(fma2(pair2(s[2 * e], s[2 * e + 1]), scale2, neg2), a, c);
       a = ex2_ftz(a);
       c = ex2_ftz(c);
+      const uint32_t w = Mma<DT>::pack(a, c);
+      unpack2(w, (DT*)nullptr, a, c);
       ls[e & 1] = add2(ls[e & 1], pair2(a, c));
-      pw[h / 2 + e] = Mma<DT>::pack(a, c);
+      pw[h / 2 + e] = w;
     }
   }
   float l0, l1;

@@ -1,4 +1,6 @@
-"""pa_decode_tree where its tiles meet their limits: values that are not finite over several checked tiles."""
+"""pa_decode_tree where its tiles and weights meet their limits: values that are not finite over several checked tiles,
+weights next to a rounding border."""
+import math
 import os
 import sys
 
@@ -52,4 +54,32 @@ def test_values_in_three_to_five_checked_tiles(pa, cuda_device, heads, prefix, n
             assert (out.double().numpy()[~ok] == want[~ok]).all(), f"{heads} {new} x {times}"
             check(torch.where(torch.from_numpy(ok), out, torch.zeros_like(out)), np.where(ok, want, 0.0),
                   f"{heads} {new} x {times}", allow=np.tile(allow, (times, 1, 1)))
+    assert pa.pa_get_error() == 0
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 128, "bf16"), (8, 1, 128, "f16"), (8, 2, 64, "bf16"), (4, 1, 64, "f16")])
+def test_a_weight_between_two_steps_that_carries_its_row(pa, cuda_device, heads):
+    """Items of more than 128 rows, weights in one 16-bit part: one token's weight is 128.5 (bf16) against a reference that
+    it does not pass by enough to move it, next to the middle of two steps. Its rounding must reach numerator and
+    denominator alike. (400 sequences, so that an item's tiles lie in one share.)"""
+    H, G, d, t = heads
+    new = 128 * G // H + 7
+    b = Batch(60, [150], [new], H, G, d, t, kind="chain")
+    weight = 128 * (1 + 0.98 * torch.finfo(b.dtype).eps / 2)
+    b.scale = math.log(weight) / 8
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k.zero_()
+    b._rows_of(b.k)[..., 0] = -48.0
+    row = torch.zeros(G, d)
+    b.set_row(0, 3, k=row.to(b.dtype), v=0.0)
+    row[:, 0] = 8.0
+    b.set_row(0, 100, k=row.to(b.dtype))
+    ref = b.reference()
+    half = torch.finfo(b.dtype).eps / 2
+    x = repeated(b, 400, cuda_device)
+    # |sum w (1 + e) v / sum w (1 + e) - out| <= half a step x sum w |v - out| / sum w (to first order in e): here
+    # (|out| + weight |v - out|) / (weight + 1), and weight (v - out) = out
+    check(x.run(pa), np.tile(ref, (400, 1, 1)), f"{heads}",
+          allow=np.tile(2 * half * np.abs(ref) / (weight + 1), (400, 1, 1)))
     assert pa.pa_get_error() == 0
