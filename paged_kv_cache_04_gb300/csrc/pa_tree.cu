@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <mutex>
 
 #include "pa_internal.h"
@@ -214,8 +215,9 @@ extern "C" pa_status pa_decode_tree(void* out, const void* q, const void* k_cach
   p.nhd = layout == PA_LAYOUT_NHD;
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  // (masked scores are infinities times the scale: a scale of zero becomes one that takes every finite score to zero)
-  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;
+  // Masked scores are infinities times the scale, so a scale of zero becomes the smallest number above it (2^-149): the
+  // largest finite score, 2^128, times that is 2^-21, which moves no weight by more than 2^-21.
+  if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::denorm_min();
   p.max_tree = max_tree_tokens;
   p.join = static_cast<TreeJoin*>(workspace);
   p.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + join_bytes());

@@ -1,5 +1,5 @@
 """pa_decode_tree where its tiles and weights meet their limits: values that are not finite over several checked tiles,
-weights next to a rounding border."""
+weights next to a rounding border, a scale of zero."""
 import math
 import os
 import sys
@@ -82,4 +82,18 @@ def test_a_weight_between_two_steps_that_carries_its_row(pa, cuda_device, heads)
     # (|out| + weight |v - out|) / (weight + 1), and weight (v - out) = out
     check(x.run(pa), np.tile(ref, (400, 1, 1)), f"{heads}",
           allow=np.tile(2 * half * np.abs(ref) / (weight + 1), (400, 1, 1)))
+    assert pa.pa_get_error() == 0
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128, "bf16"), (4, 4, 64, "f32"), (4, 2, 256, "bf16"), (8, 1, 64, "bf16")])
+def test_a_scale_of_zero_and_scores_of_any_size(pa, cuda_device, heads):
+    """Scores of up to 1e33: a plain mean all the same (their weights are off by 2^-21 at most)."""
+    H, G, d, t = heads
+    b = Batch(61, [90], [30], H, G, d, t, kind="tree")
+    b.q *= 1e16
+    b.k *= 1e16
+    b.scale = 0.0
+    ref = b.reference()
+    x = b.gpu(cuda_device)
+    check(x.run(pa), ref, f"{heads}", allow=b.allow)
     assert pa.pa_get_error() == 0
