@@ -409,14 +409,16 @@ pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t
  *                  are ignored. A node that attends nothing gives a row of zeros.
  *                  What a node does not attend never reaches its row, infinities
  *                  and NaN in the cache included.
- *   max_tree_tokens  host int >= every n_s, at most 256
+ *   max_tree_tokens  host int >= n_s of every sequence with a context, at most 256;
+ *                  mask_words is at least max_tree_tokens / 64, rounded up
  *   workspace      at least pa_decode_tree_workspace_bytes(...), 16-byte aligned;
  *                  contents ignored on entry. Calls that may overlap on the GPU
  *                  (two streams, two graphs) need one each.
  *
- * context_lens[s] = 0 gives rows of zeros, whatever n_s. A sequence with n_s
- * above max_tree_tokens or above its context, or with a range outside
- * [0, num_tokens], is left out: its rows stay as they were (PA_DEVERR_QUERY).
+ * context_lens[s] = 0 gives rows of zeros, whatever n_s (an unserved prompt's, say).
+ * A sequence with a context and n_s above max_tree_tokens or above that context, or
+ * any with a range outside [0, num_tokens], is left out: its rows stay as they were
+ * (PA_DEVERR_QUERY).
  * Block ids, contexts and types as for pa_decode (PA_F32, PA_F16, PA_BF16 caches;
  * head_dim 64, 128 or 256); E4M3 caches are not supported. Sums and softmax
  * statistics are fp32. Over 16-bit caches the softmax weights go to the tensor

@@ -83,7 +83,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeRaw& 
   t.q0 = raw.a;
   t.n = (int)((unsigned)raw.b - (unsigned)raw.a);
   t.ctx = c;
-  if (raw.a < 0 || raw.b < raw.a || raw.b > p.N || t.n > p.max_tree || (c > 0 && t.n > c)) {
+  // (without a context any number of nodes: an unserved prompt's rows are zeros, from items of one tile that reads nothing)
+  if (raw.a < 0 || raw.b < raw.a || raw.b > p.N || (c > 0 && (t.n > p.max_tree || t.n > c))) {
     bad |= kErrQuery;
     t.n = 0;
   }
@@ -217,8 +218,11 @@ __device__ __forceinline__ TreeWalk tree_share(const TreeParams& p, long long* s
     k.s = (int)scratch[WARPS];
     k.t = tree_seq(p, tree_raw(p, k.s), false);
     if (k.s + 1 < p.S) k.ahead = tree_raw(p, k.s + 1);
-    const int off = (int)scratch[WARPS + 1], per = k.t.tiles + p.item_units, idx = off / per;
-    k.w = off - idx * per;
+    const long long off = scratch[WARPS + 1];
+    const int per = k.t.tiles + p.item_units;
+    // (with a context the units of a sequence fit 31 bits, see the host's checks)
+    const int idx = off <= 0x7fffffffLL ? (int)off / per : (int)(off / per);
+    k.w = (int)(off - (long long)idx * per);
     k.kv = idx / k.t.row_tiles;
     k.rt = idx - k.kv * k.t.row_tiles;
   }

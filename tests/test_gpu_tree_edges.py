@@ -1,5 +1,5 @@
 """pa_decode_tree where its tiles and weights meet their limits: values that are not finite over several checked tiles,
-weights next to a rounding border, a scale of zero."""
+weights next to a rounding border, a scale of zero, unserved sequences."""
 import math
 import os
 import sys
@@ -97,3 +97,19 @@ def test_a_scale_of_zero_and_scores_of_any_size(pa, cuda_device, heads):
     x = b.gpu(cuda_device)
     check(x.run(pa), ref, f"{heads}", allow=b.allow)
     assert pa.pa_get_error() == 0
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128, "bf16"), (4, 4, 64, "f32"), (4, 2, 256, "f16"), (8, 8, 64, "bf16")])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+def test_an_unserved_prompt_among_drafts(pa, cuda_device, heads, kind):
+    """A context of 0 with more tokens than max_tree_tokens: rows of zeros, no error; the drafts beside it are right."""
+    H, G, d, t = heads
+    b = Batch(62, [20, 9, 0, 3000], [4, 300, 1000, 3], H, G, d, t, kind=kind)
+    b.context_lens[1] = 0
+    b.context_lens[2] = 0
+    ref = b.reference()
+    for most in (4, 64):
+        out = b.gpu(cuda_device).run(pa, most=most)
+        check(out, ref, f"{heads} {kind} most={most}")
+        assert bool((out[4:1304] == 0).all())
+        assert pa.pa_get_error() == 0
