@@ -381,7 +381,9 @@ pa_status pa_decode_split_fp8(void* out, const void* q, const void* k_cache, con
  *
  * No output may overlap an input or another output (PA_ERR_INVALID_ARG): a
  * captured loop copies or swaps the old and new arrays. num_seqs at most 4096,
- * mask_words at most 4; any block_size.
+ * mask_words at most 4; any block_size. With num_seqs 0 nothing is launched or
+ * written: a caller that goes on with padded arrays fills slot_mapping with -1 itself
+ * (the Python call does).
  */
 pa_status pa_build_tables(int32_t* block_tables, int max_blocks_per_seq, int32_t* table_lens_out,
                           int32_t* context_lens_out, int32_t* query_starts, int64_t* slot_mapping,

@@ -320,12 +320,21 @@ def pa_build_tables(block_tables, table_lens_out, context_lens_out, query_starts
 
     ``table_lens`` / ``context_lens`` hold the rows' valid entries and the cached tokens before the step; the
     ``*_out`` arrays receive those after it and may not overlap them. ``slot_mapping`` (int64 [max_tokens]) and
-    ``positions`` (int32 [max_tokens]) are filled to their end (-1 and 0 behind the last sequence's tokens).
+    ``positions`` (int32 [max_tokens]) are filled to their end (-1 and 0 behind the last sequence's tokens), for a
+    batch of no sequences too.
     """
-    (_native or _marshal()).build_tables(
+    empty = (_native or _marshal()).build_tables(
         block_tables, table_lens_out, context_lens_out, query_starts, slot_mapping, positions, free_first_out,
         table_lens, context_lens, new_lens, free_blocks, free_first, block_size, num_blocks, parents, tree_mask,
         None if stream is None else stream.cuda_stream)
+    if empty:  # nothing was launched for a batch of no sequences, but its padded arrays may still be used
+        with _torch().cuda.stream(stream):
+            slot_mapping.fill_(-1)
+            positions.zero_()
+            query_starts.zero_()
+            free_first_out.copy_(free_first.view_as(free_first_out))
+            if tree_mask is not None:
+                tree_mask.zero_()
 
 
 def pa_decode_tree_workspace_bytes(num_tokens, num_heads, num_kv_heads, head_dim, max_tree_tokens):

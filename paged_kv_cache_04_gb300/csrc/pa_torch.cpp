@@ -143,13 +143,16 @@ PyObject* guarded(const char* func, Py_ssize_t nargs, Py_ssize_t want, F body) {
   return nullptr;
 }
 
+// Returns True for a batch of no sequences, for which the library launches nothing, else None.
 PyObject* build_tables(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded("pa_build_tables", nargs, 17, [&]() -> int {
+  bool empty = false;
+  PyObject* done = guarded("pa_build_tables", nargs, 17, [&]() -> int {
     Device d;
     const Tensor& bt = tensor(a[0]);
     int32_t* bt_p = i32(d, bt);
     need(bt.dim() == 2, "block_tables must be 2-D");
     const int64_t S = bt.size(0);
+    empty = S == 0;
     auto lengths = [&](PyObject* o) {
       const Tensor& t = tensor(o);
       need(is_1d(t, S), "lengths must be [num_seqs]");
@@ -189,6 +192,9 @@ PyObject* build_tables(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                           int32(free_blocks.size(0)), ff, par_p, mask_p, words, int32(S), int32(N), int32(a[12]),
                           integer(a[13]), d.stream(a[16]));
   });
+  if (done == nullptr || !empty) return done;
+  Py_DECREF(done);
+  Py_RETURN_TRUE;
 }
 
 PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {

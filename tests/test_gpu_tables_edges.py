@@ -1,4 +1,4 @@
-"""pa_build_tables where a step's places or blocks run out, and loops of steps that go on from there."""
+"""pa_build_tables where a step's places, blocks or sequences run out, and loops of steps that go on from there."""
 import os
 import sys
 
@@ -28,6 +28,24 @@ def test_idle_sequences_behind_the_last_token_place(pa, cuda_device, tree):
         assert want["context_lens"][-1] == h["context_lens"][-1] > 0 and 0 in want["context_lens"]
         compare(run(pa, cuda_device, h, N, 1), want, 1, f"S={S}")
         assert pa.pa_get_error() == pa.PA_DEVERR_QUERY
+
+
+def test_no_sequences(pa, cuda_device):
+    """An empty batch leaves no stale slot, position, start or list entry behind."""
+    dev = cuda_device
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    empty = torch.empty(0, dtype=torch.int32, device=dev)
+    for stream in (None, torch.cuda.Stream()):
+        for tree in (False, True):
+            slots = torch.full((9,), 5, dtype=torch.int64, device=dev)
+            pos, starts, first = torch.full((9,), 5, dtype=torch.int32, device=dev), i32(7), i32(-9)
+            par, mask = (i32(*[0] * 9), torch.full((9, 2), 5, dtype=torch.int64, device=dev)) if tree else (None, None)
+            torch.cuda.synchronize()
+            pa.pa_build_tables(empty.view(0, 4), empty, empty.clone(), starts, slots, pos, first, empty, empty, empty,
+                               i32(1, 2, 3), i32(2), 16, 10, parents=par, tree_mask=mask, stream=stream)
+            torch.cuda.synchronize()
+            assert slots.tolist() == [-1] * 9 and pos.tolist() == [0] * 9 and starts.tolist() == [0]
+            assert first.tolist() == [2] and (mask is None or not mask.any())
 
 
 class KeepingServer(Server):
