@@ -177,3 +177,29 @@ def test_commit_keeps_the_lengths_of_unserved_sequences(pa, cuda_device, layers)
         assert out.tolist() == [20, 0, 40, 0]
     assert all(torch.equal(p, x.k) for p in pools)
     assert pa.pa_get_error() == 0
+
+
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_commit_skips_rows_of_blocks_outside_the_pool(pa, cuda_device, layout):
+    """A path that moves rows in a block that cannot be: recorded, that sequence's rows stay, the others' move. A path
+    that is in place moves nothing and records nothing."""
+    b = Batch(64, [20, 18, 9], [6, 6, 6], 2, 2, 64, "f16", layout=layout)
+    b.mask = torch.from_numpy(otree.pack_mask([[j in (0, 2, i) for j in range(6)] for _ in range(3) for i in range(6)], 1))
+    acc = [5, 5, 5]
+    good = b.block_tables.clone()
+    (k, v), lens = otree.commit_tree([b.k.view(torch.int16).numpy(), b.v.view(torch.int16).numpy()], good,
+                                     b.context_lens, b.query_starts, b.mask.numpy(), [5, -1, 5], 16, layout)
+    x = b.gpu(cuda_device)
+    x.block_tables[1, 1] = b.nb  # rows 18 .. 23 of the second sequence lie there
+    out = torch.full((3,), -9, dtype=torch.int32, device=cuda_device)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    pa.pa_commit_tree([x.k], [x.v], x.block_tables, x.context_lens, x.query_starts, x.mask, i32(acc), out, layout=layout)
+    assert pa.pa_get_error() == pa.PA_DEVERR_BLOCK_ID
+    assert out.tolist() == [lens[0], 18 + 3, lens[2]] == [23, 21, 12]
+    assert (x.k.cpu().view(torch.int16).numpy() == k).all() and (x.v.cpu().view(torch.int16).numpy() == v).all()
+    x = b.gpu(cuda_device)
+    x.block_tables[1, 1] = -1
+    x.mask[6:12] = 1
+    pa.pa_commit_tree([x.k], [x.v], x.block_tables, x.context_lens, x.query_starts, x.mask, i32(acc), out, layout=layout)
+    assert pa.pa_get_error() == 0 and out.tolist() == [23, 19, 12]
+    assert (x.k.cpu().view(torch.int16).numpy() == k).all() and (x.v.cpu().view(torch.int16).numpy() == v).all()
