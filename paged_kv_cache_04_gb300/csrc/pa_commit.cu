@@ -47,10 +47,11 @@ struct CommitParams {
 // moves all the list's rows of a column in order, eight loads ahead of their
 // stores (the stores of a batch end at row j + 7 < p_{j+8}, the next batch's
 // first source).
-// Bound by the chain of loads that finds the path (lengths, mask, block ids) and by the
-// moves behind it, not by bandwidth: 64 sequences x 32 layers move 30 MB in 14.5 us in a
-// graph (4.1 TB/s read and written, of 6.8); four or six rows in flight at up to 16 CTAs
-// per SM are within 1%, and slower (14.3 - 15.1 us for 14.2) on 40-head rows.
+// Bound by the chain of loads that finds the path (lengths, mask, block ids), which every
+// CTA repeats, and by the moves behind it, not by bandwidth: 64 sequences x 32 layers move
+// 27 MB in 14.7 us in a graph (54 MB read and written, 3.7 TB/s of 6.8); four or six rows
+// in flight at up to 16 CTAs per SM are within 1%, and slower (14.3 - 15.1 us for 14.2) on
+// 40-head rows.
 __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const CommitPtrs ptrs, const CommitParams p) {
   pdl_begin();
   __shared__ long long src[64 * kCommitMaxWords], dst[64 * kCommitMaxWords];  // first vector of head 0's row

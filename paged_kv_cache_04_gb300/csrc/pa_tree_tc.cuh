@@ -48,11 +48,13 @@
 // library's rule for attention, with one exception: items of more than 128 rows
 // with a 16-bit output carry them as one. There the kernel is bound by the tensor
 // cores and the softmax's instructions, not by memory: the second part doubles the
-// output products and adds 4 of 9 instructions per two weights. One part also leaves
+// output products and adds instructions for each weight (358 us against 272 on 4 x 41k
+// tokens, 64 q / 8 kv, 64 nodes; at the power limit 386 against 296). One part also leaves
 // registers to keep a tile's weights in, so its scores are read once: the weights are
 // taken against the reference so far and kept if their sum shows that none of them is
 // above 2^kTreeRescale, else the tile is read again for a new reference (a pass for
-// the maximum first: 291 us against 261 on that batch). A rounded weight w (1 + e) is
+// the maximum first: 291 us against 261 on that batch, when the sum still took the
+// weights before rounding). A rounded weight w (1 + e) is
 // off by at most half a step of the type. Sum and products take the same rounded
 // weights, so they still make an average, and to first order in e the result is off by
 //   sum w e (v - out) / sum w   <=   half a step x sum w |v - out| / sum w:
@@ -69,8 +71,9 @@
 // Measured (GB300, 2,070 MHz, attention and joining kernel, in a graph): narrow items,
 // 64 sequences of 512 to 4,096 tokens with trees of 9 to 32 nodes, 32 q / 8 kv, 118 us
 // (615 MB once: 5.2 TB/s; 5.6 TB/s of DRAM reads inside the kernel); wide ones, 4 of
-// 16k to 64k tokens with 64 nodes, 64 q / 8 kv, 261 us (1,320 TFLOP/s). A wide item's
-// tile takes about 1,800 cycles, of which its products fill 1,250: a stream's score
+// 16k to 64k tokens with 64 nodes, 64 q / 8 kv, 268 to 272 us (1,270 TFLOP/s; call after
+// call for seconds the power limit lowers the clock, 288 to 296 us). A wide item's
+// tile takes about 1,900 cycles, of which its products fill 1,250: a stream's score
 // products 386, set by the operands' 6 KB of shared memory for 32 cycles of
 // arithmetic at N = 64, its output products 257. The rest is hand-offs: a stream's
 // next scores wait for the output products of two tiles before, which wait for the
